@@ -35,7 +35,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 // and checked as the decode kernels do).
 __device__ __forceinline__ int live_parts(const MergeParams& p, int64_t row) {
     if (!p.seq_lens) return p.S;
-    int L = __ldg(p.seq_lens + row / p.rows_per_req);
+    int L = p.seq_lens[row / p.rows_per_req];
     if (L < 0 || L > p.max_pages * kPage || (L > 0 && L < p.T)) L = 0;
     const int pages = (L + kPage - 1) / kPage;
     const int n = (pages + p.chunk_pages - 1) / p.chunk_pages;
@@ -143,7 +143,7 @@ __device__ __forceinline__ void merge_row(const MergeParams& p, int64_t row, int
     auto load_part = [&](int s, uint4 (&v)[kVecs]) {
         const uint4* src = reinterpret_cast<const uint4*>(base + s * part_stride);
 #pragma unroll
-        for (int k = 0; k < kVecs; ++k) v[k] = __ldg(src + k);
+        for (int k = 0; k < kVecs; ++k) v[k] = src[k];
     };
     // The first round's values are requested together with the normalisers,
     // before the weights are known (every part s < S lies inside the buffer);

@@ -1123,17 +1123,17 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillParams p
     if (rr.seq < 0 || !prefill_seq(p, rr.seq, false).ok) return;
     const int64_t step = p.Nq * p.H;
     float top = -INFINITY;
-    for (int s = lane; s < p.n_splits; s += 32) top = fmaxf(top, __ldg(p.part_lse + s * step + w));
+    for (int s = lane; s < p.n_splits; s += 32) top = fmaxf(top, p.part_lse[s * step + w]);
 #pragma unroll
     for (int sh = 16; sh >= 1; sh >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sh));
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
     if (top > -INFINITY) {
         for (int s = 0; s < p.n_splits; ++s) {
-            const float e = __ldg(p.part_lse + s * step + w);
+            const float e = p.part_lse[s * step + w];
             if (e == -INFINITY) continue;
             const float a = ex2(e - top);
-            const float4 v = __ldg(reinterpret_cast<const float4*>(p.part_out + (s * step + w) * kPfV) + lane);
+            const float4 v = reinterpret_cast<const float4*>(p.part_out + (s * step + w) * kPfV)[lane];
             acc.x = fmaf(a, v.x, acc.x);
             acc.y = fmaf(a, v.y, acc.y);
             acc.z = fmaf(a, v.z, acc.z);

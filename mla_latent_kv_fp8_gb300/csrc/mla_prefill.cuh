@@ -52,8 +52,8 @@ struct PrefillSeq {
 
 __device__ __forceinline__ PrefillSeq prefill_seq(const PrefillParams& p, int b, bool report) {
     PrefillSeq s;
-    const int q0 = __ldg(p.cu_q + b), q1 = __ldg(p.cu_q + b + 1);
-    const int k0 = __ldg(p.cu_k + b), k1 = __ldg(p.cu_k + b + 1);
+    const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1];
+    const int k0 = p.cu_k[b], k1 = p.cu_k[b + 1];
     s.ok = q0 >= 0 && q1 >= q0 && q1 <= p.Nq && k0 >= 0 && k1 >= k0 && k1 <= p.Nk && q1 - q0 <= p.max_q &&
            k1 - k0 <= p.max_k;
     if (!s.ok && report) atomicCAS(p.err, 0, kErrSeqRange);
@@ -61,7 +61,7 @@ __device__ __forceinline__ PrefillSeq prefill_seq(const PrefillParams& p, int b,
     s.k0 = k0;
     s.nq = s.ok ? q1 - q0 : 0;
     s.nk = s.ok ? k1 - k0 : 0;
-    const int pre = p.prefix && s.ok ? __ldg(p.prefix + b) : 0;
+    const int pre = p.prefix && s.ok ? p.prefix[b] : 0;
     s.prefix = pre < 0 ? 0 : (pre > s.nk ? s.nk : pre);
     return s;
 }

@@ -13,6 +13,11 @@ namespace {
 
 // The stream's next kernel may be set up, and this one goes on when the previous
 // one has finished and its memory is visible (launch_dependent, mla_host.h).
+// Whatever an earlier kernel of the stream may have written is read after this
+// with ordinary loads: a kernel may be resident while several of its
+// predecessors still run, and the non-coherent path (__ldg) is only for memory
+// that nothing writes during the kernel's whole life.  What the wait makes
+// visible holds for ordinary loads alone.
 __device__ __forceinline__ void wait_for_previous() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -31,13 +36,13 @@ struct RaggedRow {
 // further round.  Every index stays inside cu[0..B] and start[0..B) whatever
 // the offsets hold; among empty sequences at the same offset the last one
 // that starts there (the only one that can hold the row) is found.
-__device__ __forceinline__ RaggedRow ragged_find(const int32_t* __restrict__ cu, const int32_t* __restrict__ start,
-                                                 int B, int64_t row, int lane) {
+__device__ __forceinline__ RaggedRow ragged_find(const int32_t* cu, const int32_t* start, int B, int64_t row,
+                                                 int lane) {
     int lo = 0, n = B;  // candidates [lo, lo + n)
     while (n > 32) {
         const int step = (n + 31) >> 5;
         const int off = lane * step;
-        const bool le = off < n && __ldg(cu + lo + off) <= row;
+        const bool le = off < n && cu[lo + off] <= row;
         const unsigned m = __ballot_sync(0xffffffffu, le);
         const int k = m ? 31 - __clz(m) : 0;
         lo += k * step;
@@ -45,9 +50,9 @@ __device__ __forceinline__ RaggedRow ragged_find(const int32_t* __restrict__ cu,
     }
     int32_t c = 0, e = 0, s = 0;
     if (lane < n) {
-        c = __ldg(cu + lo + lane);
-        e = __ldg(cu + lo + lane + 1);
-        if (start) s = __ldg(start + lo + lane);
+        c = cu[lo + lane];
+        e = cu[lo + lane + 1];
+        if (start) s = start[lo + lane];
     }
     const unsigned m = __ballot_sync(0xffffffffu, lane < n && c <= row && row < e);
     if (m == 0) return {-1, 0, 0};

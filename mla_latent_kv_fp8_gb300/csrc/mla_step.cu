@@ -62,19 +62,19 @@ __device__ __forceinline__ void keep_packed(uint4& v) { asm volatile("" : "+r"(v
 __device__ __forceinline__ void load_weight8(const void* w, bool f32, int at, float (&x)[8]) {
     if (f32) {
         const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + at);
-        const float4 a = __ldg(p), b = __ldg(p + 1);
+        const float4 a = p[0], b = p[1];
         x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
     } else {
-        unpack8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + at)), x);
+        unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + at), x);
     }
 }
 
 __device__ __forceinline__ void load_weight4(const void* w, bool f32, int at, float* x) {
     if (f32) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + at));
+        const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(w) + at);
         x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
     } else {
-        const uint2 a = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + at));
+        const uint2 a = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + at);
         x[0] = lo_f(a.x), x[1] = hi_f(a.x), x[2] = lo_f(a.y), x[3] = hi_f(a.y);
     }
 }
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(256, 5) append_rotated_kernel(const AppendPara
     uint4 v0 = *reinterpret_cast<const uint4*>(src + 8 * lane);
     uint4 v1 = *reinterpret_cast<const uint4*>(src + 256 + 8 * lane);
     const uint4 vr = lane < 8 ? load_pairs<kInter>(src + kDv, lane) : make_uint4(0, 0, 0, 0);
-    const Divider by_scale(__ldg(p.kv_scale));
+    const Divider by_scale(*p.kv_scale);
     const RaggedRow r = ragged_find(p.cu, p.start, p.B, row, lane);
     if (r.seq < 0) return;
     const int64_t pos = (int64_t)r.start + r.at;
@@ -199,8 +199,8 @@ __global__ void __launch_bounds__(256, 5) append_rotated_kernel(const AppendPara
         return;
     }
     const float4* cs = reinterpret_cast<const float4*>(p.cos_sin + pos * kRope);
-    const float4 c4 = __ldg(cs + (lane & 7)), s4 = __ldg(cs + 8 + (lane & 7));
-    const int32_t page = __ldg(p.block_table + r.seq * p.bt_stride + pos / kPage);
+    const float4 c4 = cs[lane & 7], s4 = cs[8 + (lane & 7)];
+    const int32_t page = p.block_table[r.seq * p.bt_stride + pos / kPage];
     if (page < 0 || page >= p.num_pages) {
         if (lane == 0) atomicCAS(p.err, 0, kErrPageRange);
         return;
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(256, 5) rotate_query_kernel(const RotateParams
         return;
     }
     const float4* cs = reinterpret_cast<const float4*>(p.cos_sin + pos * kRope);
-    const float4 c4 = __ldg(cs + l), s4 = __ldg(cs + 8 + l);
+    const float4 c4 = cs[l], s4 = cs[8 + l];
     float xr[8];
     if constexpr (kNorm != 0) {
         // The values stay packed between the sum of squares and their scaling: 40
@@ -385,7 +385,7 @@ __global__ void gather_latent_kernel(const GatherParams p) {
     const int lane = threadIdx.x & 31;
     const int64_t row = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     if (row >= p.rows) return;
-    const float scale = __ldg(p.kv_scale);
+    const float scale = *p.kv_scale;
     const RaggedRow r = ragged_find(p.cu, p.start, p.B, row, lane);
     if (r.seq < 0) return;
     const int64_t pos = (int64_t)r.start + r.at;
@@ -393,7 +393,7 @@ __global__ void gather_latent_kernel(const GatherParams p) {
     if (pos < 0 || pos >= (int64_t)p.max_pages * kPage) {
         if (lane == 0) atomicCAS(p.err, 0, kErrSeqRange);
     } else {
-        const int32_t page = __ldg(p.block_table + r.seq * p.bt_stride + pos / kPage);
+        const int32_t page = p.block_table[r.seq * p.bt_stride + pos / kPage];
         if (page < 0 || page >= p.num_pages) {
             if (lane == 0) atomicCAS(p.err, 0, kErrPageRange);
         } else {
@@ -404,7 +404,7 @@ __global__ void gather_latent_kernel(const GatherParams p) {
     uint4 v[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-        v[i] = src && 32 * i + lane < kChunks ? __ldg(reinterpret_cast<const uint4*>(src) + 32 * i + lane)
+        v[i] = src && 32 * i + lane < kChunks ? reinterpret_cast<const uint4*>(src)[32 * i + lane]
                                               : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {

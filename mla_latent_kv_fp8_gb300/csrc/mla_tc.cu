@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kLptThreads, 1) lpt_order_kernel(const DecodeP
     const int B = p.B, chunk = p.chunk_pages, n_splits = p.n_splits;
     int L = 0, full = 0, rem = 0;
     if (tid < B) {
-        L = __ldg(p.seq_lens + tid);
+        L = p.seq_lens[tid];
         if (L < 0 || L > p.max_pages * kPage || (L > 0 && L < p.T)) {
             atomicCAS(p.err, 0, kErrSeqRange);
             L = 0;
@@ -232,8 +232,8 @@ __device__ __forceinline__ bool decode_unit(const CUtensorMap* tmap, const CUten
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap_box)) : "memory");
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
         }
-        pid_cur = pg_begin + lane < p.max_pages ? __ldg(bt_cta + lane) : 0;
-        pid_nxt = pg_begin + 32 + lane < p.max_pages ? __ldg(bt_cta + 32 + lane) : 0;
+        pid_cur = pg_begin + lane < p.max_pages ? bt_cta[lane] : 0;
+        pid_nxt = pg_begin + 32 + lane < p.max_pages ? bt_cta[32 + lane] : 0;
     } else {
 #pragma unroll
         for (int rr = 0; rr < 2; ++rr) {
@@ -242,12 +242,12 @@ __device__ __forceinline__ bool decode_unit(const CUtensorMap* tmap, const CUten
 #pragma unroll
             for (int k = 0; k < 3; ++k) {
                 const int c = lane + 32 * k;  // 16-byte chunk: 8 bf16 values
-                qv[rr][k] = (r < kNq && r < HTc && c < kDqk / 8) ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                qv[rr][k] = (r < kNq && r < HTc && c < kDqk / 8) ? src[c] : make_uint4(0, 0, 0, 0);
             }
         }
     }
-    int L = L_known >= 0 ? L_known : __ldg(p.seq_lens + b);
-    const float kv_scale = __ldg(p.kv_scale);
+    int L = L_known >= 0 ? L_known : p.seq_lens[b];
+    const float kv_scale = *p.kv_scale;
     if (L < 0 || L > p.max_pages * kPage || (L > 0 && L < p.T)) {
         if (tid == 0) atomicCAS(p.err, 0, kErrSeqRange);
         L = 0;
@@ -403,7 +403,7 @@ __device__ __forceinline__ bool decode_unit(const CUtensorMap* tmap, const CUten
             for (int i = issued; i < n_pages; ++i) {
                 if ((i & 31) == 0) {  // next window of page ids; prefetch the one after
                     pid_cur = pid_nxt;
-                    pid_nxt = i + 32 + lane < n_pages ? __ldg(bt_cta + i + 32 + lane) : 0;
+                    pid_nxt = i + 32 + lane < n_pages ? bt_cta[i + 32 + lane] : 0;
                 }
                 const int32_t pid = __shfl_sync(0xffffffffu, pid_cur, i & 31);
                 if (!warp_wait(&S.empty[i % kStages], ((i / kStages) & 1) ^ 1, abort, p.err)) break;
@@ -538,13 +538,13 @@ __device__ __forceinline__ bool decode_unit(const CUtensorMap* tmap, const CUten
         }
         bool fail = false;
         int k = 0;
-        int32_t pid_next = g < n_pages ? __ldg(bt + g) : 0;
+        int32_t pid_next = g < n_pages ? bt[g] : 0;
         const float ref_shift = p.ref_shift;
         for (int i = g; i < n_pages; i += kGroups, ++k) {
             const int sb = i % kSBufs;           // score buffer
             const int kb = k & 1;                // this group's probability / statistics buffer
             const int32_t pid = pid_next;
-            if (i + kGroups < n_pages) pid_next = __ldg(bt + i + kGroups);
+            if (i + kGroups < n_pages) pid_next = bt[i + kGroups];
             const bool page_ok = pid >= 0 && pid < p.num_pages;
             const int pos = (pg_begin + i) * kPage + pr;
             float s[kHL];
@@ -812,7 +812,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5;
     // Launched as a programmatic dependent of the previous kernel on the stream:
-    // everything before this point overlaps its tail; nothing is read before it.
+    // everything before this point overlaps its tail; nothing is read before it.  Everything is read with ordinary loads: the
+    // previous kernels may still write the query or the page ids while this one is
+    // resident, and the non-coherent path (__ldg) could then return older values.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     bool tmem_held;  // the unit had pages (its set-up allocated TMEM)
     if constexpr (!kLpt) {

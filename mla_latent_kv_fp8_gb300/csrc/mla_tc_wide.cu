@@ -163,7 +163,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int HT = p.H * p.T;
     // Programmatic dependent of the previous kernel on the stream: nothing is
-    // read before this point.
+    // read before this point.  Everything is read with ordinary loads: the
+    // previous kernels may still write the query or the page ids while this one is
+    // resident, and the non-coherent path (__ldg) could then return older values.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // G = p.row_ctas CTAs per (partition, request), adjacent in the grid, CTA r
     // taking rows [r * p.rows_per_cta, ...): they run at the same time, so all
@@ -202,8 +204,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_box)) : "memory");
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap)) : "memory");
         }
-        pid_cur = pg_begin + lane < p.max_pages ? __ldg(bt_cta + lane) : 0;
-        pid_nxt = pg_begin + 32 + lane < p.max_pages ? __ldg(bt_cta + 32 + lane) : 0;
+        pid_cur = pg_begin + lane < p.max_pages ? bt_cta[lane] : 0;
+        pid_nxt = pg_begin + 32 + lane < p.max_pages ? bt_cta[32 + lane] : 0;
     } else {
 #pragma unroll
         for (int rr = 0; rr < kQR; ++rr) {
@@ -212,12 +214,12 @@ __global__ void __launch_bounds__(kWThreads, 1)
 #pragma unroll
             for (int k = 0; k < 3; ++k) {
                 const int c = lane + 32 * k;  // 16-byte chunk: 8 bf16 values
-                qv[rr][k] = (r < HTc && c < kDqk / 8) ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                qv[rr][k] = (r < HTc && c < kDqk / 8) ? src[c] : make_uint4(0, 0, 0, 0);
             }
         }
     }
-    int L = L_known >= 0 ? L_known : __ldg(p.seq_lens + b);
-    const float kv_scale = __ldg(p.kv_scale);
+    int L = L_known >= 0 ? L_known : p.seq_lens[b];
+    const float kv_scale = *p.kv_scale;
     if (L < 0 || L > p.max_pages * kPage || (L > 0 && L < p.T)) {
         if (tid == 0) atomicCAS(p.err, 0, kErrSeqRange);
         L = 0;
@@ -366,7 +368,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
             for (int i = issued; i < n_pages; ++i) {
                 if ((i & 31) == 0) {  // next window of page ids; prefetch the one after
                     pid_cur = pid_nxt;
-                    pid_nxt = i + 32 + lane < n_pages ? __ldg(bt_cta + i + 32 + lane) : 0;
+                    pid_nxt = i + 32 + lane < n_pages ? bt_cta[i + 32 + lane] : 0;
                 }
                 const int32_t pid = __shfl_sync(0xffffffffu, pid_cur, i & 31);
                 if (!warp_wait(&S.empty[i % kWStages], ((i / kWStages) & 1) ^ 1, abort, p.err)) break;
@@ -490,12 +492,12 @@ __global__ void __launch_bounds__(kWThreads, 1)
             lim[j] = grow0 + j >= HTc ? -1 : (causal ? S.rowlim[grow0 + j] : INT_MAX);
         }
         bool fail = false;
-        int32_t pid_next = __ldg(bt);
+        int32_t pid_next = bt[0];
         const float ref_shift = p.ref_shift;
         for (int i = 0; i < n_pages; ++i) {
             const int sb = i % kWSBufs, kb = i % kWPBufs, par = i & 1;
             const int32_t pid = pid_next;
-            if (i + 1 < n_pages) pid_next = __ldg(bt + i + 1);
+            if (i + 1 < n_pages) pid_next = bt[i + 1];
             const bool page_ok = pid >= 0 && pid < p.num_pages;
             const int pos = (pg_begin + i) * kPage + pr;
             const bool in_part = page_ok && pos < p_end;
