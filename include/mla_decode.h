@@ -356,9 +356,11 @@ MLA_API mla_status_t mla_gather_latent(const mla_tensor_t *kv_cache, const float
  *   out         bf16 [Nq, H, 128], rows.
  *   lse         fp32 [Nq, H], contiguous, or NULL.
  *
- * A query that sees no key gets out = 0, lse = -inf.  Rows outside the
- * sequences may hold anything, NaN included; the keys and values of a sequence
- * must be finite (a hidden key's NaN can reach rows that do not see it).
+ * A query that sees no key gets out = 0, lse = -inf.  A query whose scores are
+ * not numbers (it holds a NaN) gets NaN in out and lse; no other row changes.
+ * Rows outside the sequences may hold anything, NaN included; the keys and
+ * values of a sequence must be finite (a hidden key's NaN can reach rows that
+ * do not see it).
  * Scores, normalisers and sums are fp32; the probabilities are rounded to bf16
  * for the product with v.  Split partials use the library's scratch of the
  * stream (see the note on threading above).

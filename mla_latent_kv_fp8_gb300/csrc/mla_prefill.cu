@@ -853,7 +853,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) tmem_ld32(ts + 32 * j, sv[j]);
                 tmem_wait_ld();
+                // the tile row's visible keys among the 32 of group j, as bits
+                auto visible = [&](int j) {
+                    const int at = key0 + 32 * j;
+                    return (low_bits(row_hi - at) & ~low_bits(row_lo - at)) | low_bits(a.prefix - at);
+                };
                 if constexpr (kCap) {
+                    // The cap below would make a number of a NaN.  A NaN or an infinity in a
+                    // query makes every score of its row one, so one score tells whether to
+                    // look at all; a visible NaN then goes into the sum and so into out and lse.
+                    if (__any_sync(0xffffffffu, !(fabsf(__uint_as_float(sv[0][0])) < INFINITY))) {
+                        bool bad = false;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t see = visible(j);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) bad |= (see >> k & 1) && isnan(__uint_as_float(sv[j][k]));
+                        }
+                        if (bad) l = NAN;
+                    }
                     // cap tanh(s / cap) = cap + 2 cap u with u = -1 / (1 + e^(2 s / cap)): u is
                     // the score from here on, scale 2 cap, and the constant joins lse at
                     // the end (u is off by up to 7 2^-24).  One reciprocal serves four scores
@@ -885,8 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!clear) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const int at = key0 + 32 * j;
-                        const uint32_t see = (low_bits(row_hi - at) & ~low_bits(row_lo - at)) | low_bits(a.prefix - at);
+                        const uint32_t see = visible(j);
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
                             if (!(see >> k & 1)) sv[j][k] = __float_as_uint(-INFINITY);
@@ -1021,9 +1038,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l_odd = l;
                     continue;
                 }
-                // O of the tile times f0 plus, in halves, O of tile 1 times f1
+                // O of the tile times f0 plus, in halves, O of tile 1 times f1.  (A sum is 0
+                // for a row that saw no key; a NaN is an answer and stays one.)
                 float f0 = 1.f, f1 = 0.f;
-                const bool join = __any_sync(0xffffffffu, l_odd > 0.f), some = __any_sync(0xffffffffu, l > 0.f);
+                const bool join = __any_sync(0xffffffffu, l_odd != 0.f), some = __any_sync(0xffffffffu, l != 0.f);
                 if (join) {
                     const float top = fmaxf(m, m_odd);
                     if (top > -INFINITY) {
@@ -1033,8 +1051,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l = l * f0 + l_odd * f1;
                     m = top;
                 }
-                const float inv = l > 0.f ? 1.f / l : 0.f;
-                const float lse2 = l > 0.f ? m * scale + (kCap ? kLog2e * p.cap : 0.f) + log2f(l) : -INFINITY;
+                const float inv = l != 0.f ? 1.f / l : 0.f;
+                const float lse2 = l != 0.f ? m * scale + (kCap ? kLog2e * p.cap : 0.f) + log2f(l) : -INFINITY;
                 f0 *= inv;
                 f1 *= inv;
                 const int at = kRows * t + r;
@@ -1128,24 +1146,22 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillParams p
     for (int sh = 16; sh >= 1; sh >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sh));
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
-    if (top > -INFINITY) {
-        for (int s = 0; s < p.n_splits; ++s) {
-            const float e = p.part_lse[s * step + w];
-            if (e == -INFINITY) continue;
-            const float a = ex2(e - top);
-            const float4 v = reinterpret_cast<const float4*>(p.part_out + (s * step + w) * kPfV)[lane];
-            acc.x = fmaf(a, v.x, acc.x);
-            acc.y = fmaf(a, v.y, acc.y);
-            acc.z = fmaf(a, v.z, acc.z);
-            acc.w = fmaf(a, v.w, acc.w);
-            sum += a;
-        }
+    for (int s = 0; s < p.n_splits; ++s) {
+        const float e = p.part_lse[s * step + w];
+        if (e == -INFINITY) continue;
+        const float a = ex2(e - top);  // (a part that is NaN stays NaN: the maximum passes over it)
+        const float4 v = reinterpret_cast<const float4*>(p.part_out + (s * step + w) * kPfV)[lane];
+        acc.x = fmaf(a, v.x, acc.x);
+        acc.y = fmaf(a, v.y, acc.y);
+        acc.z = fmaf(a, v.z, acc.z);
+        acc.w = fmaf(a, v.w, acc.w);
+        sum += a;
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
     const int h = static_cast<int>(w - row * p.H);
     *reinterpret_cast<uint2*>(p.out + row * p.out_tok + h * p.out_head + 4 * lane) =
         make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-    if (p.lse && lane == 0) p.lse[w] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+    if (p.lse && lane == 0) p.lse[w] = sum != 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {

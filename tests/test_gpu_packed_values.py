@@ -1,0 +1,105 @@
+"""Values at the edges of the packed operators' ranges: NaN and infinities in a query, signed zeros, unusual scales and
+caps, and every combination of weight type and layout."""
+import math
+
+import pytest
+import torch
+
+from tests import ragged_reference as R
+from tests.test_gpu_ragged import SCALE, _cu, _dev, _prefill, _prefill_inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def L():
+    from mla_latent_kv_fp8_gb300 import build
+    build.build()
+    from mla_latent_kv_fp8_gb300 import _lib
+    _lib.lib()
+    assert _lib.mla_device_error() == 0
+    return _lib
+
+
+# ---------------------------------------------------------------- NaN and infinities in a query
+
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+@pytest.mark.parametrize("n_splits", [1, 4])
+@pytest.mark.parametrize("lq,lk", [([1], [40]), ([100], [900]), ([3, 260], [700, 2100]), ([40] * 40, [50] * 40)])
+def test_nan_queries_give_nan_and_nothing_else_changes(L, lq, lk, n_splits, cap):
+    """A NaN in one dim, in the rotated dims, and in all of a query row: NaN in out and lse of that row and head, not
+    the answer of a row without a key and not an ordinary number; every other row is the same bit for bit."""
+    H, n = 2, sum(lq)
+    q, kn, kp, v = _prefill_inputs(lq, lk, H, 500 + n, pad=2)
+    want, want_lse = _prefill(L, (q, kn, kp, v), lq, lk, n_splits, cap)
+    rows = sorted({0, n // 2, n - 1})
+    bad = torch.zeros((n + 2, H), dtype=torch.bool, device="cuda")
+    q = q.clone()
+    for at, (row, dims) in enumerate(zip(rows, (slice(5, 6), slice(150, 151), slice(0, 192)))):
+        q[row, at % H, dims] = math.nan
+        bad[row, at % H] = True
+    out, lse = _prefill(L, (q, kn, kp, v), lq, lk, n_splits, cap)
+    torch.cuda.synchronize()
+    assert L.mla_device_error() == 0
+    assert bool(out[bad].isnan().all()) and bool(lse[bad].isnan().all())
+    assert torch.equal(out[~bad], want[~bad]) and torch.equal(lse[~bad], want_lse[~bad])
+
+
+@pytest.mark.parametrize("n_splits", [1, 3])
+@pytest.mark.parametrize("n", [1, 300])
+def test_infinite_queries(L, n, n_splits):
+    """One infinity in a query: its scores are infinities of both signs.  Without a cap the softmax is not a number;
+    with one they are +-cap.  Two infinities of opposite signs: not a number either way."""
+    H, cap, keys = 1, 20.0, 800
+    q, kn, kp, v = _prefill_inputs([n], [keys], H, 600 + n)
+    kn = kn.clone()
+    kn[:, 0, 3] = torch.where(kn[:, 0, 3] == 0, 1.0, kn[:, 0, 3])
+    q[n // 2, 0, 3] = math.inf
+    for c, nan in ((0.0, True), (cap, False)):
+        out, lse = _prefill(L, (q, kn, kp, v), [n], [keys], n_splits, c, causal=0)
+        torch.cuda.synchronize()
+        row, z = out[n // 2, 0].double(), lse[n // 2, 0].double()
+        if nan:
+            assert bool(row.isnan().all()) and bool(z.isnan())
+            continue
+        s = cap * torch.sign(kn[:, 0, 3].double())
+        p = torch.softmax(s, 0)
+        ref, ref_z = p @ v[:, 0].double(), torch.logsumexp(s, 0)
+        # the scores are off by at most cap * 2^-20, probabilities are rounded to bf16 and so is the output
+        e = cap * 2.0 ** -20
+        assert bool(((row - ref).abs() <= (p @ v[:, 0].double().abs()) * (R.BF16_HALF + 2 * e + 2.0 ** -12)
+                     + R.BF16_HALF * 1.01 * ref.abs()).all())
+        assert abs(float(z - ref_z)) <= 2 * e + 2.0 ** -21 * float(ref_z) + 2.0 ** -18
+    q[n // 2, 0, 4] = -math.inf
+    same = kn[:, 0, 3] * kn[:, 0, 4] > 0             # inf - inf in these keys' scores
+    assert bool(same.any())
+    out, lse = _prefill(L, (q, kn, kp, v), [n], [keys], n_splits, cap, causal=0)
+    torch.cuda.synchronize()
+    assert L.mla_device_error() == 0
+    assert bool(out[n // 2].isnan().all()) and bool(lse[n // 2].isnan().all())
+    rest = torch.arange(n, device="cuda") != n // 2
+    assert not bool(out[rest].isnan().any()) and not bool(lse[rest].isnan().any())
+
+
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+def test_nan_scores_of_hidden_keys_only(L, cap):
+    """Scores that are not numbers, but only at keys that the row does not see (past its place under the causal mask, and
+    past the sequence's end): the row's answer is an ordinary one."""
+    H, n, pad = 1, 200, 100
+    q, kn, kp, v = _prefill_inputs([n], [n], H, 71, pad=pad)     # rows past the sequence are NaN and infinities
+    kn = kn.clone()
+    q[50, 0, :2] = torch.tensor([math.inf, -math.inf])           # inf - inf where k[0] k[1] > 0
+    kn[:n, 0, 0] = 1.0
+    kn[:n, 0, 1] = torch.where(torch.arange(n, device="cuda") <= 50, -1.0, 1.0)   # visible: +inf, hidden: NaN
+    out, lse = _prefill(L, (q, kn, kp, v), [n], [n], 1, cap)
+    torch.cuda.synchronize()
+    assert L.mla_device_error() == 0
+    if cap:                                                       # all 51 visible scores are the cap
+        ref = v[:51, 0].double().mean(0)
+        bound = v[:51, 0].double().abs().mean(0) * (2 * R.BF16_HALF + 2.0 ** -12) + R.BF16_HALF * ref.abs()
+        assert bool(((out[50, 0].double() - ref).abs() <= bound).all())
+        assert abs(float(lse[50, 0]) - (cap + math.log(51))) <= cap * 2.0 ** -19 + 2.0 ** -18
+    else:
+        assert bool(out[50].isnan().all()) and bool(lse[50].isnan().all())
+    assert not bool(out[51:n].isnan().any()) and not bool(out[:50].isnan().any())
+    assert bool((out[n:] == 7).all())
