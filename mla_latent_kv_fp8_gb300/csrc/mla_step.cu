@@ -170,7 +170,8 @@ struct Divider {
     __device__ __forceinline__ float operator()(float x) const {
         if (!plain) return __fdiv_rn(x, s);
         const float q = x * inv;
-        return fabsf(q) < 1024.f ? fmaf(fmaf(-q, s, x), inv, q) : q;
+        // (the remainder with this sign: of a signed zero it is +0 and its negative -0, which keeps q's sign)
+        return fabsf(q) < 1024.f ? fmaf(-fmaf(q, s, -x), inv, q) : q;
     }
 };
 

@@ -21,6 +21,34 @@ def L():
     return _lib
 
 
+# ---------------------------------------------------------------- codes
+
+def _append_both(L, latent, scale):
+    """The codes of latent rows [n, 576] by mla_append_rotated (no norm, angles of 0) and by mla_append_latent."""
+    n = latent.shape[0]
+    table = torch.zeros((n, 64), device="cuda")
+    table[:, :32] = 1
+    pages = -(-n // 64)
+    bt, start = torch.arange(pages, dtype=torch.int32, device="cuda")[None], _dev([0])
+    a = torch.full((pages, 64, 576), 0xAA, dtype=torch.uint8, device="cuda")
+    b = a.clone()
+    sc = _dev([scale], torch.float32)
+    L.mla_append_rotated(latent, None, 0.0, table, 1, _dev([0, n]), sc, bt, start, a)
+    L.mla_append_latent(latent[None], sc, bt, start, b)
+    torch.cuda.synchronize()
+    assert L.mla_device_error() == 0
+    return a.view(-1, 576)[:n], b.view(-1, 576)[:n]
+
+
+def test_codes_of_signed_zeros(L):
+    """-0 keeps its sign, as a division does."""
+    latent = torch.zeros((2, 576), dtype=torch.bfloat16, device="cuda")
+    latent[1, :512] = -0.0
+    a, b = _append_both(L, latent, 0.031)
+    assert torch.equal(a, b)
+    assert bool((a[0] == 0).all()) and bool((a[1, :512] == 0x80).all())
+
+
 # ---------------------------------------------------------------- NaN and infinities in a query
 
 @pytest.mark.parametrize("cap", [0.0, 20.0])
