@@ -1,5 +1,5 @@
 """Values at the edges of the packed operators' ranges: NaN and infinities in a query, signed zeros, unusual scales and
-caps, and every combination of weight type and layout."""
+caps."""
 import math
 
 import pytest
@@ -47,6 +47,32 @@ def test_codes_of_signed_zeros(L):
     a, b = _append_both(L, latent, 0.031)
     assert torch.equal(a, b)
     assert bool((a[0] == 0).all()) and bool((a[1, :512] == 0x80).all())
+
+
+@pytest.mark.parametrize("scale", [
+    0.031, 1.0, 1.53173798, 0.0113, 448.0, 3e-5, float.fromhex("0x1.881dfcp+0"),
+    float.fromhex("0x1.00000ap+3"), float.fromhex("0x1.1fffeep-5"), float.fromhex("0x1.fffff4p-1"),  # near 2^20 multiples
+    2.0 ** -90, 2.0 ** 90, float.fromhex("0x1.fffffep-91"), float.fromhex("0x1.000002p+90"),        # ends of the fast range
+    1e-38, 1e-42, 3e38, 0.0, -0.02, math.inf, -math.inf, math.nan,                                  # the general division
+])
+def test_codes_are_those_of_a_plain_division(L, scale):
+    """Byte for byte those of mla_append_latent, whatever the scale: values around every border between codes and
+    random ones, zeros, infinities and NaN of both signs, the smallest and the largest numbers."""
+    unit = scale if 0 < abs(scale) < math.inf else 1.0
+    t = torch.arange(16, 32, dtype=torch.float64)
+    border = torch.cat([t * 2.0 ** e for e in range(-14, 6)])
+    x = torch.cat([border * unit * (1 + d * 2.0 ** -8) for d in range(-2, 3)]
+                  + [torch.randn(20000, dtype=torch.float64, generator=torch.Generator().manual_seed(1)) * unit * g
+                     for g in (0.01, 1.0, 100.0)]
+                  + [torch.tensor([0.0, math.inf, math.nan, 2.0 ** -133, 3e38, 2.0 ** -126])])
+    x = torch.cat([x, -x])
+    rows = -(-len(x) // 512)
+    latent = torch.ones((rows, 576), dtype=torch.float64)
+    flat = torch.zeros(rows * 512, dtype=torch.float64)
+    flat[:len(x)] = x
+    latent[:, :512] = flat.view(rows, 512)
+    a, b = _append_both(L, latent.to(torch.bfloat16).cuda(), scale)
+    assert torch.equal(a, b)
 
 
 # ---------------------------------------------------------------- NaN and infinities in a query
