@@ -1,12 +1,12 @@
 """Values at the edges of the packed operators' ranges: NaN and infinities in a query, signed zeros, unusual scales and
-caps."""
+caps, and every combination of weight type and layout."""
 import math
 
 import pytest
 import torch
 
 from tests import ragged_reference as R
-from tests.test_gpu_ragged import SCALE, _cu, _dev, _prefill, _prefill_inputs
+from tests.test_gpu_ragged import SCALE, _cu, _dev, _prefill, _prefill_inputs, _randn
 
 pytestmark = pytest.mark.gpu
 
@@ -157,3 +157,51 @@ def test_nan_scores_of_hidden_keys_only(L, cap):
         assert bool(out[50].isnan().all()) and bool(lse[50].isnan().all())
     assert not bool(out[51:n].isnan().any()) and not bool(out[:50].isnan().any())
     assert bool((out[n:] == 7).all())
+
+
+# ---------------------------------------------------------------- every weight type and layout
+
+WEIGHTS = [None, torch.bfloat16, torch.float32]
+
+
+def _weight(dims, dtype, seed):
+    if dtype is None:
+        return None
+    return (1 + 0.2 * torch.randn(dims, generator=torch.Generator().manual_seed(seed))).to(dtype)
+
+
+@pytest.mark.parametrize("dtype", WEIGHTS)
+@pytest.mark.parametrize("interleaved", [0, 1])
+@pytest.mark.parametrize("n", [1, 70, 2500])
+def test_append_forms(L, dtype, interleaved, n):
+    latent, weight, scale = _randn((n, 576), 3 * n), _weight(512, dtype, n), 0.0123
+    table, past = R.cos_sin(n + 30), 30
+    pages = -(-(n + past) // 64)
+    cache = torch.zeros((pages, 64, 576), dtype=torch.uint8, device="cuda")
+    kept = torch.zeros((n, 576), dtype=torch.bfloat16, device="cuda")
+    L.mla_append_rotated(latent.cuda(), weight.cuda() if weight is not None else None, 1e-6, table.cuda(), interleaved,
+                         _dev([0, n]), _dev([scale], torch.float32),
+                         torch.arange(pages, dtype=torch.int32, device="cuda")[None], _dev([past]), cache, kept)
+    torch.cuda.synchronize()
+    assert L.mla_device_error() == 0
+    ref, size = R.new_latents(latent, weight, 1e-6, table, interleaved, torch.arange(n) + past)
+    sc = float(torch.tensor(scale))
+    R.assert_bf16(kept.cpu(), ref, size, "kept")
+    R.assert_codes(cache.cpu().view(-1, 576)[past:past + n], ref / sc, size / sc, "codes")
+
+
+@pytest.mark.parametrize("dtype", WEIGHTS)
+@pytest.mark.parametrize("interleaved", [0, 1])
+@pytest.mark.parametrize("n,H", [(1, 1), (33, 12), (700, 5)])
+def test_rotate_forms(L, dtype, interleaved, n, H):
+    q, weight, table = _randn((n, H, 192), 7 * n + H), _weight(192, dtype, n), R.cos_sin(n + 9)
+    nope = torch.zeros((n, H, 128), dtype=torch.bfloat16, device="cuda")
+    pe = torch.zeros((n, H, 64), dtype=torch.bfloat16, device="cuda")
+    L.mla_rotate_query(q.cuda(), weight.cuda() if weight is not None else None, 1e-6, table.cuda(), interleaved,
+                       _dev([0, n]), _dev([9]), nope, pe)
+    torch.cuda.synchronize()
+    assert L.mla_device_error() == 0
+    x = q.double() if weight is None else R.norm(q.double(), weight, 1e-6)
+    ref, size = R.rotate(x[..., 128:], table[torch.arange(n) + 9][:, None], interleaved)
+    R.assert_bf16(pe.cpu(), ref, size, "rotated")
+    R.assert_bf16(nope.cpu(), x[..., :128], x[..., :128].abs(), "other dims")
