@@ -349,7 +349,8 @@ MLA_API mla_status_t mla_gather_latent(const mla_tensor_t *kv_cache, const float
  *               0: choose (mla_prefill_auto_splits).
  *   sm_scale    > 0, finite.
  *   softcap     0 (no cap), or in [2^-10, 4096]: a capped score is computed to
- *               within softcap * 2^-20 (2^-23 on average).
+ *               within softcap * 2^-20 (2^-23 on average) for a cap up to 64,
+ *               and to within 2^-20 of itself, by a slower path, for a larger one.
  *   causal      0 or 1.  window >= 0; 0: none.
  *   prefix_lens i32 [B], device, or NULL: leading keys that every query sees
  *               (clamped to [0, Lk]).

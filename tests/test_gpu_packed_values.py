@@ -159,6 +159,42 @@ def test_nan_scores_of_hidden_keys_only(L, cap):
     assert bool((out[n:] == 7).all())
 
 
+# ---------------------------------------------------------------- caps
+
+@pytest.mark.parametrize("cap", [2.0 ** -10, 0.05, 1.0, 64.0, 64.5, 300.0, 4096.0])
+@pytest.mark.parametrize("n_splits,most", [(1, 2), (3, 2), (1, 24)])
+def test_caps_over_their_range(L, cap, n_splits, most):
+    """Scores small and large against the cap, from whole numbers, so that the products and their sums are exact in fp32
+    and what is left is the cap: out and lse are as close as its stated accuracy lets them be."""
+    lq, lk, H, scale = [300, 5], [900, 130], 2, 1 / 16
+    q, kn, kp, v = _prefill_inputs(lq, lk, H, 41)
+    g = torch.Generator().manual_seed(most)
+    whole = lambda shape, m: torch.randint(-m, m + 1, shape, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    q, kn, kp = whole(q.shape, most), whole(kn.shape, 2), whole(kp.shape, 2)
+    cu_q, cu_k = _cu(lq), _cu(lk)
+    out = torch.empty((sum(lq), H, 128), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((sum(lq), H), device="cuda")
+    L.mla_prefill_ragged(q, kn, kp, v, _dev(cu_q), _dev(cu_k), max(lq), max(lk), n_splits, scale, cap, 0, 0, None, out, lse)
+    torch.cuda.synchronize()
+    assert L.mla_device_error() == 0
+    ref, z, _, _ = R.prefill(q, kn, kp, v, cu_q, cu_k, scale, cap, False)
+    for b in range(2):
+        rows, keys = slice(cu_q[b], cu_q[b + 1]), slice(cu_k[b], cu_k[b + 1])
+        for h in range(H):
+            k = torch.cat([kn[keys, h].double(), kp[keys].double()], 1)
+            s = cap * torch.tanh(q[rows, h].double() @ k.T * scale / cap)
+            # a score: its cap as documented, and a few roundings of its multiples and of the reference it is held
+            # against, relative to it (to the cap, where it is held as a difference to the cap)
+            e = (2.0 ** -20 + 8 * R.F32_HALF) * (cap if cap <= 64 else s.abs().amax(1)) + 2.0 ** -20
+            e = torch.as_tensor(e, device="cuda").expand(s.shape[0])
+            p = torch.softmax(s, 1)
+            bound = (p @ v[keys, h].double().abs()) * (R.BF16_HALF + 2 * e[:, None] + 2.0 ** -12) \
+                + R.BF16_HALF * 1.01 * ref[rows, h].abs() + 1e-30
+            assert bool(((out[rows, h].double() - ref[rows, h]).abs() <= bound).all())
+            lse_bound = 2 * e + 2.0 ** -21 * z[rows, h].abs() + 2.0 ** -18
+            assert bool(((lse[rows, h].double() - z[rows, h]).abs() <= lse_bound).all())
+
+
 # ---------------------------------------------------------------- every weight type and layout
 
 WEIGHTS = [None, torch.bfloat16, torch.float32]
