@@ -445,7 +445,7 @@ MLA_API int32_t mla_last_decode_impl(void);
 
 /* Synchronise `stream`, then read and clear the device error word of the
  * current device: 0 means no kernel reported an error.  Codes: 1 a bounded
- * wait timed out, 2 a page id out of range, 3 a seq_len out of range. */
+ * wait timed out (the outputs of its call are undefined), 2 a page id out of range, 3 a seq_len out of range. */
 MLA_API mla_status_t mla_device_error(int32_t *code, void *stream);
 
 /* Benchmark instrumentation: the next mla_decode_paged call made by the

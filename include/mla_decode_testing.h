@@ -3,8 +3,9 @@
  * Not part of the decode operation: one exercises its failure detection, the
  * other measures the memory ceiling of its access pattern.
  *
- * Every wait inside the tensor-core decode kernel is bounded (2 s).  When a
- * wait runs out, the kernel records MLA device error 1 (wait timeout, read
+ * Every wait inside the tensor-core decode kernels and the ragged prefill is
+ * bounded (2 s; 60 s for those of the prefill that may last as long as a work
+ * item).  When a wait runs out, the kernel records MLA device error 1 (wait timeout, read
  * with mla_device_error), stops its other roles, drains what it has in
  * flight, frees its tensor memory and returns; the CUDA context stays usable.
  */
@@ -19,10 +20,10 @@
 extern "C" {
 #endif
 
-/* on != 0: every later tensor-core decode launch made from the CALLING
- * THREAD (other threads are unaffected) issues no page copies, so each of its
- * waits for a page runs out after 2 s and the launch ends with device error
- * 1; its outputs are undefined.  on == 0 restores normal operation.  Returns
+/* on != 0: every later tensor-core decode or ragged prefill launch made from
+ * the CALLING THREAD (other threads are unaffected) issues no copies, so each
+ * of its waits for a page or a key block runs out after 2 s and the launch ends
+ * with device error 1; its outputs are undefined.  on == 0 restores normal operation.  Returns
  * the previous setting of this thread.  Host-side only: nothing on the GPU
  * faults, traps or hangs. */
 MLA_API int mla_test_stall_copies(int on);

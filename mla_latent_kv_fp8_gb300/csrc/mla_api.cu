@@ -197,6 +197,7 @@ mla_status_t internal_check_tensor(const mla_tensor_t* t, const char* name, int 
     return check_tensor(t, name, ndim, dtype, need_contig, align);
 }
 mla_status_t internal_scratch(size_t need, cudaStream_t stream, void** out) { return get_scratch(need, stream, out); }
+int internal_test_stall() { return t_test_stall; }
 
 mla_status_t internal_prepare_decode(const mla_tensor_t* q, const mla_tensor_t* kv_cache, const float* kv_scale,
                                      const mla_tensor_t* block_table, const mla_tensor_t* seq_lens,

@@ -36,6 +36,9 @@ mla_status_t internal_check_rows(const mla_tensor_t* t, const char* name, int nd
 // ownership, growth and capture).
 mla_status_t internal_scratch(size_t need, cudaStream_t stream, void** out);
 
+// Whether the calling thread's launches issue no copies (mla_test_stall_copies).
+int internal_test_stall();
+
 // Checks the arguments of a decode call (mla_decode_paged and
 // mla_decode_paged_noalloc take the same ones) and fills *p with everything
 // but the split scratch: shapes, pointers, the resolved partition count

@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 s = (s + 1) % kSlots;
                 return dst;
             };
-            for (int item = 0; ok; ++item) {
+            for (int item = 0; ok && !p.test_stall_copies; ++item) {
                 const int sl = item % kPlans;
                 if (!wait_bounded(&S.plan_full[sl], (item / kPlans) & 1, abort, p.err)) break;
                 const Plan a = S.plan[sl];

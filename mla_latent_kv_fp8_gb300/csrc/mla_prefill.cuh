@@ -40,6 +40,7 @@ struct PrefillParams {
     float* part_out;
     float* part_lse;
     int* err;
+    int test_stall_copies;               // failure-detection tests only: issue no copies
 };
 
 // One sequence of the batch: its rows and lengths.  ok is false, and the

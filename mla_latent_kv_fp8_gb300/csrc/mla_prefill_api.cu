@@ -186,6 +186,7 @@ mla_status_t mla_prefill_ragged(const mla_tensor_t* q, const mla_tensor_t* k_nop
     p.lse = lse ? static_cast<float*>(lse->data) : nullptr;
     if (prefill_ctas(p) > 0x7fffffff || Nq * H > (int64_t(1) << 33))
         return internal_fail(MLA_ERR_UNSUPPORTED, "too many query rows for one launch");
+    p.test_stall_copies = internal_test_stall();
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (p.n_splits > 1) {
         void* ws = nullptr;
