@@ -35,12 +35,13 @@ void raise_status(int status, const char* message) {
 }
 
 // The arguments of one call, taken in order; after a bad one `ok` is false, a
-// Python exception is set and the rest is skipped.
+// Python exception is set and the rest is skipped.  The current device is asked
+// for with the first tensor: what is no tensor is refused without a GPU too.
 struct Args {
     PyObject* const* at;
     Py_ssize_t left;
     bool ok = true;
-    int device = c10::cuda::current_device();
+    int device = -1;
     mla_tensor_t desc[12];
     int used = 0;
 
@@ -62,6 +63,7 @@ struct Args {
             return nullptr;
         }
         const at::Tensor& t = THPVariable_Unpack(o);
+        if (device < 0 && t.is_cuda()) device = c10::cuda::current_device();
         if (!t.is_cuda() || t.get_device() != device) {
             raise_status(MLA_ERR_INVALID_ARG, "a tensor is not on the current CUDA device");
             ok = false;
@@ -133,7 +135,7 @@ struct Args {
         PyObject* o = next();
         if (!o) return nullptr;
         if (o == Py_None)
-            return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream();
+            return c10::cuda::getCurrentCUDAStream().stream();
         PyObject* handle = PyLong_Check(o) ? Py_NewRef(o) : PyObject_GetAttrString(o, "cuda_stream");
         if (!handle) {
             ok = false;
