@@ -1,9 +1,11 @@
-"""Build the CUDA library in-tree for sm_103a with nvcc (no cmake, no torch extension).
+"""Build the CUDA library in-tree for sm_103a with nvcc (no cmake).
 
 Each ``csrc/*.cu`` file is compiled to an object in parallel, then linked into
 ``libmla_decode.so`` next to this file; ``csrc/binding.cpp`` becomes the Python
-extension ``_packed.so`` beside it (g++, against the installed torch).  The CUDA runtime is linked statically;
-the driver API is reached through the runtime's entry-point query.
+extension ``_packed.so`` beside it (g++, against the installed torch).  The library needs nvcc alone: where the
+extension cannot be built, a warning says so, the decode and the C ABI are there all the same, and the packed operators'
+Python functions raise.  The CUDA runtime is linked statically; the driver API is reached through the runtime's
+entry-point query.
 """
 from __future__ import annotations
 
@@ -12,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -42,6 +45,13 @@ def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
+def _run(cmd):
+    try:
+        return subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:  # no such compiler
+        return subprocess.CompletedProcess(cmd, 127, "", f"{e}\n")
+
+
 def _binding_jobs(force: bool):
     """The command that compiles the Python extension's object, if it is stale."""
     import sysconfig
@@ -66,9 +76,8 @@ def _link_binding(obj: str) -> None:
     import torch
     root = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING + f".tmp{os.getpid()}"
-    r = subprocess.run(["g++", "-shared", "-o", tmp, obj, f"-L{HERE}", "-lmla_decode", "-Wl,-rpath,$ORIGIN",
-                        f"-L{root}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"],
-                       capture_output=True, text=True)
+    r = _run(["g++", "-shared", "-o", tmp, obj, f"-L{HERE}", "-lmla_decode", "-Wl,-rpath,$ORIGIN", f"-L{root}",
+              "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"])
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("linking _packed.so failed")
@@ -85,7 +94,7 @@ def _stale(out, deps):
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile (if stale) libmla_decode.so, whose path is returned, and the Python extension."""
+    """Compile (if stale) libmla_decode.so, whose path is returned, and the Python extension (or warn)."""
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
@@ -98,16 +107,22 @@ def build(force: bool = False, verbose: bool = False) -> str:
         objs.append(obj)
         if force or _stale(obj, [src, *headers, __file__]):
             jobs.append([nvcc, *_flags(vptx), "-c", src, "-o", obj])
-    binding, binding_obj = _binding_jobs(force)
     kernels = list(jobs)
+    try:
+        binding, binding_obj = _binding_jobs(force)
+    except Exception as e:  # no torch, or one without headers
+        binding, binding_obj = [], None
+        problem = str(e)
     jobs += binding
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
-            results = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
+            results = list(ex.map(_run, jobs))
         for cmd, r in zip(jobs, results):
             if vptx or r.returncode != 0:
                 sys.stderr.write(r.stdout + r.stderr)
-            if r.returncode != 0:
+            if r.returncode != 0 and cmd in binding:
+                binding_obj, problem = None, f"{cmd[0]} failed for {BINDING_SRC}"
+            elif r.returncode != 0:
                 raise RuntimeError(f"{cmd[0]} failed for {cmd[-3]}")
     if force or kernels or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
@@ -117,8 +132,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("linking libmla_decode.so failed")
         os.replace(tmp, LIB)
-    if binding or _stale(BINDING, [binding_obj]):
-        _link_binding(binding_obj)
+    if binding_obj and (binding or _stale(BINDING, [binding_obj])):
+        try:
+            _link_binding(binding_obj)
+        except (RuntimeError, OSError) as e:
+            binding_obj, problem = None, str(e)
+    if binding_obj is None:
+        if os.path.exists(BINDING):  # of another source or torch
+            os.remove(BINDING)
+        warnings.warn(f"the Python extension of the packed operators was not built: {problem}", RuntimeWarning)
     return LIB
 
 
