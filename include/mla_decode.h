@@ -347,7 +347,8 @@ MLA_API mla_status_t mla_gather_latent(const mla_tensor_t *kv_cache, const float
  *   n_splits    > 0: cut the keys of every block of query rows into this many
  *               parts (at most 256) whose partial answers are then merged;
  *               0: choose (mla_prefill_auto_splits).
- *   sm_scale    > 0, finite.
+ *   sm_scale    > 0, at most 2^20; without a cap no score may exceed 2^30 in
+ *               size (its row is not a number then).
  *   softcap     0 (no cap), or in [2^-10, 4096]: a capped score is computed to
  *               within softcap * 2^-20 (2^-23 on average) for a cap up to 64,
  *               and to within 2^-20 of itself, by a slower path, for a larger one.

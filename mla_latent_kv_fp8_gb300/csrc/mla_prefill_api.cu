@@ -139,6 +139,9 @@ mla_status_t mla_prefill_ragged(const mla_tensor_t* q, const mla_tensor_t* k_nop
     if (n_splits < 0 || n_splits > 256) return internal_fail(MLA_ERR_INVALID_ARG, "n_splits must lie in [0, 256]");
     if (!(sm_scale > 0.f) || !std::isfinite(sm_scale))
         return internal_fail(MLA_ERR_INVALID_ARG, "sm_scale must be finite and > 0");
+    // A row's largest score times log2(e) is held in fp32; beyond 2^31 its rounding exceeds what an exponential can
+    // take, and the answer is not a number (scores of 2^30 are told apart by 64, which is a weight of 0 or 1).
+    if (sm_scale > 0x1p20f) return internal_fail(MLA_ERR_UNSUPPORTED, "sm_scale must be at most 2^20");
     if (!(softcap >= 0.f)) return internal_fail(MLA_ERR_INVALID_ARG, "softcap must be >= 0");
     if (softcap != 0.f && (softcap < 0x1p-10f || softcap > 4096.f))
         return internal_fail(MLA_ERR_UNSUPPORTED, "softcap must be 0 (none) or lie in [2^-10, 4096]");

@@ -195,6 +195,40 @@ def test_caps_over_their_range(L, cap, n_splits, most):
             assert bool(((lse[rows, h].double() - z[rows, h]).abs() <= lse_bound).all())
 
 
+@pytest.mark.parametrize("cap", [0.0, 2.0 ** -10])
+def test_smallest_and_largest_scales(L, cap):
+    """A scale so small that every score is 0: the mean of the values; the largest one: the value of the best key (with
+    a cap, where every score is +-cap: finite)."""
+    n, keys, H = 130, 300, 2
+    q, kn, kp, v = _prefill_inputs([n], [keys], H, 81)
+    outs = []
+    for scale in (2.0 ** -100, 2.0 ** 20):
+        out = torch.empty((n, H, 128), dtype=torch.bfloat16, device="cuda")
+        lse = torch.empty((n, H), device="cuda")
+        L.mla_prefill_ragged(q, kn, kp, v, _dev([0, n]), _dev([0, keys]), n, keys, 1, scale, cap, 0, 0, None, out, lse)
+        torch.cuda.synchronize()
+        assert L.mla_device_error() == 0
+        outs.append((out.double(), lse.double()))
+    mean = v.double().mean(0)
+    # probabilities of 2^0, exact in bf16; sums of 300 fp32 terms; the output's rounding
+    bound = R.BF16_HALF * 1.01 * mean.abs() + 300 * R.F32_HALF * v.double().abs().mean(0) + 2.0 ** -20 * cap
+    assert bool(((outs[0][0] - mean).abs() <= bound).all())
+    assert bool(((outs[0][1] - math.log(keys)).abs() <= 2.0 ** -18).all())
+    out, lse = outs[1]
+    assert not bool(out.isnan().any()) and bool(lse.isfinite().all())
+    if cap == 0:
+        k = torch.cat([kn.double(), kp.double()[:, None].expand(-1, H, -1)], -1)
+        s = torch.einsum("nhd,mhd->nhm", q.double(), k)
+        size = torch.einsum("nhd,mhd->nhm", q.double().abs(), k.abs()).amax(2)
+        two = s.topk(2, 2).values
+        sure = two[..., 0] - two[..., 1] > 2 * 200 * R.F32_HALF * size      # more than the products' sums may be off
+        best = v.double().permute(1, 0, 2)[torch.arange(H, device="cuda")[None], s.argmax(2)]
+        # The best key's probability is 2^d before the division by the sum, d the rounding of the reference (scores of
+        # 2^26 have a step of 4): out is v * bf16(2^d) / 2^d, off by up to half a bf16 step, and rounded once more.
+        near = (out - best).abs() <= (2 * R.BF16_HALF + R.BF16_HALF ** 2) * best.abs()
+        assert bool(sure.float().mean() > 0.9) and bool(near[sure].all())
+
+
 # ---------------------------------------------------------------- every weight type and layout
 
 WEIGHTS = [None, torch.bfloat16, torch.float32]
