@@ -38,7 +38,8 @@
  * Scratch that a captured call used is not freed when the stream's scratch
  * grows, so the graph stays valid after later, larger calls on the stream; a
  * graph replayed on another stream still uses the scratch of the stream it was
- * captured on.  mla_release_graph_scratch() frees such scratch once the graphs
+ * captured on: it must not overlap on the GPU with calls on that stream, nor
+ * with another graph captured there.  mla_release_graph_scratch() frees such scratch once the graphs
  * that used it are gone.
  *
  * Errors: every entry point validates its arguments on the host before any
@@ -375,15 +376,19 @@ MLA_API mla_status_t mla_prefill_ragged(const mla_tensor_t *q, const mla_tensor_
                                 const mla_tensor_t *out, const mla_tensor_t *lse, void *stream);
 
 /* The automatic split count used when n_splits == 0, from the sizes the host
- * knows: the count whose estimated time is the shortest -- the longest part of
- * 256 query rows against the whole work spread over the SMs, plus the writing
- * and joining of the partial answers; parts have at least 512 keys.
+ * knows.  The prefill takes its query rows in items of 256 or of 128 and picks
+ * the size and the count together, those whose estimated time is the shortest:
+ * the longest part of an item against the whole work spread over the SMs, plus
+ * the writing and joining of the partial answers.  The longest part of the
+ * longest item has at least four blocks of 128 keys; other parts may be shorter
+ * or empty.  max_q and max_k are the longest sequence's (0 gives 1).
  * Pure host function; sm_count <= 0 means "query the current device". */
 MLA_API int32_t mla_prefill_auto_splits(int64_t Nq, int32_t B, int32_t H, int32_t max_q, int32_t max_k,
                                 int32_t causal, int32_t window, int32_t sm_count);
 
-/* Bytes of library scratch one mla_prefill_ragged call with these sizes uses
- * (0 when n_splits is 1). */
+/* Bytes of library scratch one mla_prefill_ragged call with these sizes and
+ * this count uses (0 when n_splits is 1; for the automatic count pass what
+ * mla_prefill_auto_splits returns). */
 MLA_API size_t mla_prefill_workspace_bytes(int64_t Nq, int32_t H, int32_t n_splits);
 
 /* The automatic split count used when n_splits == 0, from max_pages alone
