@@ -42,18 +42,19 @@
 // 12-15 output.  A softmax thread holds a row of 128 scores: the other warps
 // hand registers over (128 x 64 + 128 x 80 + 256 x 184 = 512 x 128, what the
 // launch has; with 72 and 72 the output warps spilled: 4 x 1,000 tokens x 12
-// heads 28.8 us, with 64 and 80 28.0).
+// heads 28.8 us, with 64 and 80 28.0.  The kernel with packed caps still spills
+// five registers, the others none).
 // Every wait is bounded; on a timeout the kernel sets the error word, drains
 // its copies and products, frees its tensor memory and returns.
 //
-// Measured on a GB300 (graph replays; the products alone at the rate of a large
-// library product, 1,861 TFLOP/s, would take 554 us in the first case):
-// 16,384 causal tokens x 12 heads 562 us (1,830 TFLOP/s, bound by the tensor
-// core and the power limit); 16 documents, 8,192 tokens 48 us, 4,000 tokens 50
+// Measured on a GB300 (bursts of graph replays; the products alone at the rate of
+// a large library product, 1,861 TFLOP/s, would take 554 us in the first case):
+// 16,384 causal tokens x 12 heads 560 us (1,840 TFLOP/s, bound by the tensor core
+// and the power limit, which makes it 630 in calls back to back); 16 documents, 8,192 tokens 48 us, 4,000 tokens 50
 // and 300 tokens over 98,000 191: bound by the chain score - softmax - product of
 // a tile block, ~2,850 cycles of which the products are 1,280, and by the start
 // and end of items; with a cap by a chain of twice that length, 2,000 cycles of it
-// for the cap (8,192 tokens x 12 heads 276 us, without the cap 160).
+// for the cap (8,192 tokens x 12 heads 276 us, without the cap 159).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>

@@ -287,8 +287,11 @@ struct RotateParams {
 // 4l .. 4l + 3.  Everything of a head is read before any of it is written, by
 // the same lane at the same place, so the outputs may be the input's own dims.
 // Bound by memory (it reads and writes the same bytes, like a copy): 8,191
-// tokens x 96 heads with a norm 93 us, 6.5 TB/s; 48 registers and 40 warps an
-// SM (64 registers 107 us, 40 with spills 100).
+// tokens x 96 heads with a norm 93 us, 6.5 TB/s, in both layouts; 48 registers
+// and 40 warps an SM (64 registers 107 us, 40 with spills 100; the interleaved
+// layout with a norm spills four to six of the 48).  Without a norm only a third
+// of each head is read, 128 of 384 bytes, and written as 128-byte rows of a wider
+// tensor: 53 us for the 203 MB, 3.8 TB/s.
 // kNorm: 0 none, 1 with bf16 weights, 2 with fp32 weights.
 template <bool kInter, int kNorm>
 __global__ void __launch_bounds__(256, 5) rotate_query_kernel(const RotateParams p) {
@@ -320,8 +323,8 @@ __global__ void __launch_bounds__(256, 5) rotate_query_kernel(const RotateParams
     const float4 c4 = cs[l], s4 = cs[8 + l];
     float xr[8];
     if constexpr (kNorm != 0) {
-        // The values stay packed between the sum of squares and their scaling: 40
-        // registers a thread, 48 warps an SM.
+        // The values stay packed between the sum of squares and their scaling, which
+        // is what lets 48 registers do.
         float x[8], weight[8];
         float ss = sum_squares(v0) + sum_squares(v1) + sum_squares(vr);
 #pragma unroll
