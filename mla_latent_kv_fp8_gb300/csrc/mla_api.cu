@@ -142,6 +142,8 @@ mla_status_t get_scratch(size_t need, cudaStream_t stream, void** out) {
 }
 
 bool contiguous(const mla_tensor_t* t) {
+    for (int i = 0; i < t->ndim; ++i)
+        if (t->shape[i] == 0) return true;  // no element, whatever its strides
     int64_t expect = 1;
     for (int i = t->ndim - 1; i >= 0; --i) {
         if (t->shape[i] != 1 && t->stride[i] != expect) return false;

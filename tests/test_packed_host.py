@@ -1,7 +1,7 @@
 """Host-side checks of the packed operators (no GPU needed), beside those of test_ragged_host.py."""
 import pytest
 
-from tests.test_ragged_host import L, _prefill  # noqa: F401 (L is a fixture)
+from tests.test_ragged_host import F32, L, _prefill, _strided  # noqa: F401 (L is a fixture)
 
 
 @pytest.mark.parametrize("scale,status", [(2.0 ** 21, 2), (2.0 ** 100, 2), (3e38, 2), (float("inf"), 1)])
@@ -27,3 +27,9 @@ def test_automatic_splits_leave_the_longest_part_four_blocks(L, causal, window):
                         keys = min(max_k, window + min(max_q, rows)) if window else max_k
                         longest = max(longest, -(-(-(-keys // 128)) // n))
                     assert n == 1 or longest >= 4
+
+
+def test_tensors_without_elements_are_contiguous(L):  # noqa: F811
+    """An lse [5, 0] of a call without heads, its strides as torch gives them (1, 1)."""
+    assert _prefill(L, H=0, lse=_strided([5, 0], [1, 1], F32)) == 0
+    assert _prefill(L, lse=_strided([5, 3], [1, 1], F32)) == 2      # with elements they have to be
